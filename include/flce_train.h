@@ -70,8 +70,9 @@ int flce_qk_norm_rope_forward(const flce_qk_shape* shape, const flce_qk_view* q,
  * back, xh = x rstd and g = d gamma:
  *   dx = rstd (g - xh mean_j(g xh)),    dgamma = sum over tokens and heads of d xh
  * dq / dk are written (they may be the same views as dq_out / dk_out); dgamma_q / dgamma_k [D] fp32
- * are written, or added to with accumulate_dgamma = 1, and may be NULL (not wanted).  dgamma is
- * summed in a fixed order: per block of the launch in `workspace`, then over the blocks.
+ * are written, or added to with accumulate_dgamma = 1, and may be NULL (not wanted); they must not
+ * overlap each other (FLCE_ERR_ARG): one gamma for queries and keys takes two gradients, whose sum is
+ * its own.  dgamma is summed in a fixed order: per block of the launch in `workspace`, then over the blocks.
  * workspace: flce_qk_norm_rope_workspace_bytes(shape) bytes, 256-byte aligned; contents on entry
  * ignored.  Without rows, dgamma is zero.
  */

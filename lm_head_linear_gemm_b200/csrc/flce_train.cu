@@ -75,6 +75,13 @@ int qk_shape_ok(const flce_qk_shape* s) {
   return FLCE_OK;
 }
 
+// Two arrays of n floats that share an element; NULL shares none.
+bool floats_overlap(const float* a, const float* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t bytes = static_cast<uintptr_t>(n) * sizeof(float);
+  return a != nullptr && b != nullptr && (x < y ? y - x : x - y) < bytes;
+}
+
 // A view of H heads: alignment, and for a written one that no two elements share a place.
 int qk_view_ok(const flce_qk_shape* s, const flce_qk_view* v, int64_t H, bool written) {
   if (v == nullptr) return H == 0 ? FLCE_OK : FLCE_ERR_ARG;
@@ -425,6 +432,8 @@ int flce_qk_norm_rope_backward(const flce_qk_shape* s, const flce_qk_view* dq_ou
   if (!aligned(workspace, 256) || !aligned(dgamma_q, 4) || !aligned(dgamma_k, 4))
     return FLCE_ERR_ALIGN;
   if (workspace_bytes < flce_qk_norm_rope_workspace_bytes(s)) return FLCE_ERR_WORKSPACE;
+  // the two sums are stored by different warps: in one place they would overwrite each other
+  if (floats_overlap(dgamma_q, dgamma_k, s->D)) return FLCE_ERR_ARG;
   int device = 0, sms = 0;
   FLCE_TRY(device_sms(&device, &sms));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -137,7 +137,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, inv_freq, posi
                           stream=None):
     """Chain rule of qk_norm_rope_forward for the gradients of its outputs.  Returns
     (dq, dk, dgamma_q, dgamma_k); the gammas' gradients are float32, written or (with
-    ``accumulate_dgamma``) added to, and None where there is no gamma."""
+    ``accumulate_dgamma``) added to, and None where there is no gamma.  ``dgamma_q`` and ``dgamma_k``
+    may not be one buffer, even where gamma_q and gamma_k are: add the two."""
     inputs = (q, k, gamma_q, gamma_k, inv_freq, positions, eps, interleaved)
     with on_stream(stream, q.device):
         made = _abi.marshal().qk_backward(*inputs, dq_out, dk_out, dq, dk, dgamma_q, dgamma_k,
