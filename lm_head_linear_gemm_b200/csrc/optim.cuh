@@ -786,13 +786,15 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(
   if (tid == 0) args.partial[blockIdx.x] = sum;
 }
 
+// The launch before still writes the partials while this one starts, so they are no read-only data
+// of this kernel: no __restrict__, and loads from L2 (__ldcg) behind the wait.
 __global__ void __launch_bounds__(kNormThreads) grad_norm_finish_kernel(
-    const double* __restrict__ partial, long long parts, float max_norm, float* norm_out,
-    float* factor_out) {
+    const double* partial, long long parts, float max_norm, float* norm_out, float* factor_out) {
   __shared__ double s_sum[kNormThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the partials are complete
   double sum = 0.0;
-  for (long long i = threadIdx.x; i < parts; i += kNormThreads) sum += partial[i];
+  for (long long i = threadIdx.x; i < parts; i += kNormThreads)
+    sum += __ldcg(partial + i);
   sum = norm_block_sum(sum, s_sum);
   if (threadIdx.x != 0) return;
   const float norm = static_cast<float>(sqrt(sum));

@@ -561,17 +561,20 @@ __global__ void __launch_bounds__(32 * kQkWarps, kQkBlocks)
 }
 
 // dgamma (+)= the blocks' partials, 32 columns to a block of 32 x 32 threads: thread row y sums the
-// parts y, y + 32, ... in order, then a warp sums a column's 32 by a fixed tree.
-__global__ void __launch_bounds__(1024) qk_dgamma_kernel(const float* __restrict__ partial,
-                                                         int parts, int D, float* dgamma_q,
-                                                         float* dgamma_k, int accumulate) {
+// parts y, y + 32, ... in order, then a warp sums a column's 32 by a fixed tree.  The launch before
+// still writes the partials while this one starts, so they are no read-only data of this kernel:
+// no __restrict__, and loads from L2 (__ldcg) behind the wait.
+__global__ void __launch_bounds__(1024) qk_dgamma_kernel(const float* partial, int parts, int D,
+                                                         float* dgamma_q, float* dgamma_k,
+                                                         int accumulate) {
   __shared__ float s_sum[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the partials are complete
   const int e = blockIdx.x * 32 + threadIdx.x;             // of 2 D columns: q's, then k's
   float acc = 0.f;
   if (e < 2 * D) {
 #pragma unroll 4
-    for (int b = threadIdx.y; b < parts; b += 32) acc += partial[static_cast<size_t>(b) * 2 * D + e];
+    for (int b = threadIdx.y; b < parts; b += 32)
+      acc += __ldcg(partial + static_cast<size_t>(b) * 2 * D + e);
   }
   s_sum[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
