@@ -298,7 +298,7 @@ __device__ __forceinline__ void encode_states(const float (&m)[8], const float (
     qm = encode8(q, 1.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      q[i] = r[i] != 0.f && rs != 0.f
+      q[i] = v[i] != 0.f && rs != 0.f            // the approximate root of a v below 2^-126 is 0
                  ? max_abs3(__fdiv_rn(__fsqrt_rn(v[i]), rs), 0.001953125f, 0.f)
                  : 0.f;
     qr = encode8(q, 1.f);

@@ -287,6 +287,27 @@ def test_small_second_moments_keep_a_code(cuda_device):
     assert bool((p.abs() <= 3 * 0.1 * 1.2).all())         # steps stay near lr
 
 
+def test_second_moments_below_the_normal_range_keep_a_code(cuda_device):
+    """v below 2^-126, which the approximate root takes for 0, keeps its code: the largest of a block
+    448, a small one next to a large one the smallest.  g = 1e-19 and c2 = 0.04 give v = 2^-130.9,
+    known to half of 2^-149: its root is off by under 2^-19, the scale by 8 u more."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    g = torch.full((512,), 1e-19, device="cuda")
+    g[256], g[300], g[3] = 1.0, 0.0, 0.0
+    p = torch.zeros(512, device="cuda")
+    opt = flce.AdamW([p], state_bits=8, min_8bit_size=0, **GROUP)
+    opt.step([g])
+    r, scale = opt.state[0]["r"].float(), opt.state[0]["r_scale"]
+    want = torch.full((512,), 448.0, device="cuda")
+    want[257:] = 2.0 ** -9
+    want[300] = want[3] = 0
+    assert torch.equal(r, want)
+    root = float(torch.tensor(1e-19)) * 0.04 ** 0.5
+    assert abs(float(scale[0]) * 448 / root - 1) <= 2.0 ** -19 + 8 * U
+    assert bool((opt.state[0]["m"].float()[g > 0] != 0)[:255].all())
+
+
 def test_skip_on_a_factor_that_is_not_finite(cuda_device):
     import torch
     import lm_head_linear_gemm_b200 as flce
