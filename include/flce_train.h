@@ -95,9 +95,11 @@ int flce_qk_norm_rope_backward(const flce_qk_shape* shape, const flce_qk_view* d
  *
  * States in 8 bits (FLCE_STATE_E4M3): m and r = sqrt(v) are e4m3 codes with an fp32 scale for
  * every FLCE_STATE_BLOCK consecutive elements of the tensor (the last block may be shorter):
- *   scale = amax / 448, or 0 where that is below 2^-126 (the block then holds zeros);
+ *   scale = amax * (1/448 rounded to fp32), rounded: at most one unit of the last place from
+ *     the rounded amax / 448; 0 where it is below 2^-126 (the block then holds zeros);
  *   code = e4m3(x / scale), nearest even;  an r > 0 gets at least the smallest code, so that a
- *   denominator never vanishes next to a first moment that does not.
+ *     denominator does not vanish next to a first moment that does not (the next step's v, the
+ *     square of code * scale, is 0 only where that is below 2^-75).
  * The step itself uses m and v before they are rounded.
  */
 enum { FLCE_STATE_F32 = 0, FLCE_STATE_E4M3 = 1 };

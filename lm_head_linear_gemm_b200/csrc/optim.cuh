@@ -222,7 +222,8 @@ __device__ __forceinline__ float block_max(const float (&f)[8]) {
   for (int i = 0; i < 8; i += 2) top = max_abs3(top, f[i], f[i + 1]);
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
-// amax / 448, or 0 where that is below 2^-126: its reciprocal has to be finite.
+// amax times the rounded 1/448, as the format defines it (a division would cost more and differ by one
+// unit of the last place at most), or 0 where that is below 2^-126: its reciprocal has to be finite.
 __device__ __forceinline__ float scale_of(float amax) {
   const float scale = amax * (1.f / 448.f);
   return scale < 1.17549435e-38f ? 0.f : scale;

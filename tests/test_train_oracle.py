@@ -81,3 +81,15 @@ def test_block_scales_and_norm():
     norm, factor = ot.grad_norm([np.full(9, 2.0), np.array([8.0])], 1.0)
     assert norm == 10.0 and abs(factor - 1 / (10 + 1e-6)) <= 1e-15
     assert ot.grad_norm([np.ones(1)], 5.0)[1] == 1.0
+
+
+def test_scale_as_a_product_is_one_unit_from_the_quotient():
+    """The 8-bit format's scale, amax times 1/448 rounded to fp32: 1/448 is off by 0.75 2^-24 of
+    itself, at most 0.75 units of the product's last place, which rounding turns into one at most."""
+    rng = np.random.default_rng(9)
+    x = (rng.random(1 << 20) + 1).astype(np.float32)
+    c = np.float32(1 / 448)
+    assert abs(float(c) * 448 - 1) <= 0.751 * 2.0 ** -24
+    product, quotient = x * c, x / np.float32(448)
+    apart = np.abs(product.view(np.int32) - quotient.view(np.int32))
+    assert apart.max() == 1
