@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 from array import array
+from ctypes import c_float
 from types import MappingProxyType
 
 import torch
@@ -209,7 +210,8 @@ class AdamW:
     def step(self, grads=None, grad_scale=None, stream=None):
         """One step.  ``grads``: a list in the order of ``params`` (all groups' parameters one after
         the other) with None for a parameter to leave alone; default ``self.grads()``.
-        ``grad_scale`` multiplies every gradient: a float or a one-element float32 device tensor."""
+        ``grad_scale`` multiplies every gradient: a float (in a captured step its value stays) or a
+        one-element float32 device tensor."""
         grads = self.grads() if grads is None else list(grads)
         n, dev = len(self.params), self.device
         pointers, types, places = _abi.marshal().gradients(grads, self.params, dev.index,
@@ -222,6 +224,10 @@ class AdamW:
             self._grad_types = types
         with on_stream(stream, dev), on_device(dev):
             handle = torch._C._cuda_getCurrentRawStream(dev.index)
+            if grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
+                # a fill, not a copy from the host: nothing waits, and a capture may hold it
+                grad_scale = torch.full((), c_float(grad_scale).value, dtype=torch.float32,
+                                        device=dev)
             grad_scale = _abi._grad_scale(grad_scale, dev)
             rc = _abi.lib().flce_adamw_step(
                 self._tensors, pointers, n, self._groups(),

@@ -360,6 +360,40 @@ def test_captured_steps_count_and_read_the_rate(cuda_device):
         assert all(torch.equal(s[k].view(torch.uint8), r[k].view(torch.uint8)) for k in s)
 
 
+@pytest.mark.parametrize("scale", [0.5, 0.1, 2])
+def test_a_number_as_the_factor_waits_for_nothing(cuda_device, scale):
+    """A factor given as a number is filled in on the device: a step with it may be captured, and an
+    eager one does not wait for what the stream still has to do."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    g = torch.randn(300, device="cuda")
+    made = [torch.ones(300, device="cuda") for _ in range(3)]
+    opts = [flce.AdamW([p]) for p in made]
+    opts[0].step([g], grad_scale=torch.tensor(float(scale), device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opts[1].step([g], grad_scale=scale)
+    graph.replay()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                        # about 0.1 s
+    opts[2].step([g], grad_scale=scale)
+    assert not torch.cuda.current_stream().query()
+    assert torch.equal(made[0], made[1]) and torch.equal(made[0], made[2])
+
+
+def test_numbers_beyond_fp32_as_the_factor(cuda_device):
+    """They are infinite on the device, and the step is skipped."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    p = torch.ones(300, device="cuda")
+    opt = flce.AdamW([p])
+    for scale in (1e39, float("inf"), float("nan")):
+        opt.step([p.clone()], grad_scale=scale)
+    assert bool((p == 1).all()) and int(opt.step_count) == 0
+    with pytest.raises(TypeError):
+        opt.step([p.clone()], grad_scale="half")
+
+
 def test_eight_bit_states_take_the_definitions_roundings(cuda_device):
     """m, v, scales and codes equal, bit for bit, the definition computed by torch in fp32 one
     operation at a time; two steps, so that the second starts from the first's codes."""
