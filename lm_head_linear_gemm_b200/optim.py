@@ -251,8 +251,9 @@ class AdamW:
 
     def load_state_dict(self, saved):
         """Copies a state_dict's values into this optimizer's tensors; the layout (bits, master
-        copies, sizes) has to be this optimizer's.  A learning rate on the device is copied into
-        this optimizer's where it has one, so that a captured step follows."""
+        copies, sizes) has to be this optimizer's.  Where this optimizer's learning rate is on the
+        device, the saved one, a tensor or a number, is written into it, so that a captured step
+        follows."""
         if len(saved["state"]) != len(self.state) or len(saved["groups"]) != len(self.param_groups):
             raise ValueError("the saved optimizer has other parameters or groups")
         for mine, theirs in zip(self.state, saved["state"]):
@@ -265,10 +266,9 @@ class AdamW:
                 mine[k].copy_(theirs[k].reshape(mine[k].shape))
         for mine, theirs in zip(self.param_groups, saved["groups"]):
             for k, v in theirs.items():
-                if isinstance(v, torch.Tensor):          # a rate on the device: its own tensor stays
-                    if isinstance(mine.get(k), torch.Tensor):
-                        mine[k].copy_(v.reshape(mine[k].shape))
-                        continue
-                    v = v.to(self.device, copy=True)
-                mine[k] = v
+                own, given = mine.get(k), isinstance(v, torch.Tensor)
+                if isinstance(own, torch.Tensor):        # a rate on the device: its own tensor stays
+                    own.copy_(v.reshape(own.shape)) if given else own.fill_(v)
+                else:
+                    mine[k] = v.to(self.device, copy=True) if given else v
         self.step_count.copy_(saved["step"])

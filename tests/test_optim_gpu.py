@@ -479,6 +479,28 @@ def test_states_are_not_replaced_and_a_device_rate_is_copied(cuda_device):
     assert opt.param_groups[0]["lr"] == 0.125
 
 
+@pytest.mark.parametrize("saved_on", ["host", "device"])
+def test_a_captured_step_follows_a_loaded_rate(cuda_device, saved_on):
+    """A step captured with its rate on the device reads the rate that load_state_dict brings,
+    whether that was saved as a number or as a tensor."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    g = torch.randn(300, device="cuda")
+    rate = torch.full((1,), 0.5, device="cuda")
+    p, q = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    opt = flce.AdamW([p], lr=rate)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step([g])
+    lr = 0.125 if saved_on == "host" else torch.full((1,), 0.125, device="cuda")
+    other = flce.AdamW([q], lr=lr)
+    opt.load_state_dict(other.state_dict())
+    assert opt.param_groups[0]["lr"] is rate and float(rate) == 0.125
+    other.step([g])
+    graph.replay()
+    assert torch.equal(p, q)
+
+
 def test_optimizers_at_once_on_two_streams(cuda_device):
     import torch
     import lm_head_linear_gemm_b200 as flce
