@@ -344,6 +344,13 @@ def _check_buffer(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_memory(t, name):
+    """The library takes address 0 for an argument that is not given: a tensor whose elements lie
+    elsewhere (a wrapper, such as a sharded tensor) must not pass for one."""
+    if t.data_ptr() == 0 and t.numel():
+        raise ValueError(f"{name} must have memory of its own (a sharded tensor's local part has)")
+
+
 def _check_scalar(t, name, dtype, device):
     """A one-element device tensor (count, scale, upstream gradient)."""
     if t is None:

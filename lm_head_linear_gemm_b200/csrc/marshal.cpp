@@ -76,6 +76,10 @@ const at::Tensor* tensor_of(PyObject* o, const char* what) {
   return &THPVariable_Unpack(o);
 }
 
+// Elements without an address: a wrapper around tensors that lie elsewhere (a sharded one, say).  The
+// library takes NULL for an argument that is not given, so these must not reach it.
+bool lies_elsewhere(const at::Tensor& t) { return t.numel() > 0 && t.const_data_ptr() == nullptr; }
+
 // Its FLCE_DTYPE_*; -1 with an exception set when the library cannot read it.
 int32_t code_of(const at::Tensor& t, int device, const char* what) {
   if (!t.is_cuda() || (device >= 0 && t.get_device() != device)) {
@@ -90,6 +94,11 @@ int32_t code_of(const at::Tensor& t, int device, const char* what) {
   }
   if (t.layout() != at::kStrided || !t.is_contiguous()) {
     PyErr_Format(PyExc_ValueError, "every %s must be contiguous", what);
+    return -1;
+  }
+  if (lies_elsewhere(t)) {
+    PyErr_Format(PyExc_ValueError, "every %s must have memory of its own (a sharded tensor's local "
+                 "part has)", what);
     return -1;
   }
   return type == at::kBFloat16 ? kBf16 : kF32;
@@ -222,7 +231,7 @@ PyObject* grad_norm(PyObject* const* args, Py_ssize_t count) {
 const at::Tensor* cuda_tensor(PyObject* o) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.is_cuda() && t.layout() == at::kStrided ? &t : nullptr;
+  return t.is_cuda() && t.layout() == at::kStrided && !lies_elsewhere(t) ? &t : nullptr;
 }
 bool element_type(const at::Tensor& t, int32_t* code) {
   const auto type = t.scalar_type();

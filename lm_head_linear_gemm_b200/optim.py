@@ -30,6 +30,15 @@ def on_device(device):
     return contextlib.nullcontext() if same else torch.cuda.device(device)
 
 
+def device_scalar(t, name, device):
+    """The address of a one-element float32 tensor on the device; None for None."""
+    if t is None:
+        return None
+    _abi._check_scalar(t, name, torch.float32, device)
+    _abi._check_memory(t, name)
+    return t.data_ptr()
+
+
 def grad_norm(grads, max_norm: float | None = None, stream=None):
     """(norm, factor) of a list of gradients (None entries are left out) as one-element float32
     device tensors: the L2 norm over all of them and ``min(1, max_norm / (norm + 1e-6))``, NaN when
@@ -112,6 +121,7 @@ class AdamW:
         if step is None:
             step = torch.zeros(1, dtype=torch.int64, device=dev)
         _abi._check_buffer(step, "step", torch.int64, (1,), dev)
+        _abi._check_memory(step, "step")
         self.step_count = step
         self._scratch = torch.zeros(4, dtype=torch.int32, device=dev)
         n = len(self.params)
@@ -128,6 +138,7 @@ class AdamW:
             raise TypeError(f"parameters must be float32 or bfloat16, got {p.dtype}")
         if not p.is_contiguous():
             raise ValueError("parameters must be contiguous")
+        _abi._check_memory(p, "every parameter")
 
     @staticmethod
     def _new_state(p, eight, master):
@@ -169,6 +180,7 @@ class AdamW:
                 raise ValueError(f"{name} must have {size} elements, got {t.numel()}")
             _abi._check_buffer(t, name, code if name in ("m", "v", "r") else torch.float32,
                                tuple(t.shape), dev)
+            _abi._check_memory(t, name)
         if "master" in s and p.dtype != torch.bfloat16:
             raise ValueError("only a bfloat16 parameter takes a master copy")
         ptr = {name: t.data_ptr() for name, t in s.items()}
@@ -199,8 +211,7 @@ class AdamW:
         for o, g in zip(out, self.param_groups):
             lr = g["lr"]
             if isinstance(lr, torch.Tensor):
-                _abi._check_scalar(lr, "lr", torch.float32, self.device)
-                o.lr_device = lr.data_ptr()
+                o.lr_device = device_scalar(lr, "lr", self.device)
             else:
                 o.lr = float(lr)
             o.beta1, o.beta2 = g["betas"]
@@ -228,10 +239,9 @@ class AdamW:
                 # a fill, not a copy from the host: nothing waits, and a capture may hold it
                 grad_scale = torch.full((), c_float(grad_scale).value, dtype=torch.float32,
                                         device=dev)
-            grad_scale = _abi._grad_scale(grad_scale, dev)
             rc = _abi.lib().flce_adamw_step(
-                self._tensors, pointers, n, self._groups(),
-                len(self.param_groups), _abi._ptr(grad_scale), self.step_count.data_ptr(),
+                self._tensors, pointers, n, self._groups(), len(self.param_groups),
+                device_scalar(grad_scale, "grad_scale", dev), self.step_count.data_ptr(),
                 int(self.skip_nonfinite), self._scratch.data_ptr(), handle)
         if rc != _abi.FLCE_OK:
             raise _abi.FlceError(rc, "flce_adamw_step")

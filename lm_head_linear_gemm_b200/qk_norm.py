@@ -106,7 +106,8 @@ def _say(inputs, rows, vectors=(), accumulate=False):
         if gamma is not None and t is None and accumulate:
             raise ValueError(f"accumulate_dgamma needs {name}")
         _abi._check_buffer(t, name, torch.float32, (q.shape[-1],), q.device)
-    raise TypeError("q, k and all that goes with them must be dense CUDA tensors of torch")
+    raise TypeError("q, k and all that goes with them must be dense CUDA tensors of torch with memory "
+                    "of their own")
 
 
 def qk_norm_rope_forward(q, k, gamma_q, gamma_k, inv_freq, positions=None, eps: float = 1e-6,
