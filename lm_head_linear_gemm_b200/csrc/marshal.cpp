@@ -118,7 +118,7 @@ T* data_of(const Held& bytes) {
   return reinterpret_cast<T*>(PyBytes_AS_STRING(bytes.o));
 }
 
-// A tensor that a call is about to change in place: a graph that saved it raises instead of using the
+// A tensor that a call changes in place: a graph that saved it raises instead of using the
 // new values.
 void changes(const at::Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
@@ -127,8 +127,7 @@ void changes(const at::Tensor& t) {
 // gradients(gradients, parameters, device, types) -> (addresses, types, parameters' places): each
 // gradient, where it is not None, checked against its parameter's shape.  An entry without one has
 // address 0 and keeps its type of `types` (bytes of int32).  A place, three words, changes when the
-// parameter is given other memory, another size, type, layout or device.  The parameters with a
-// gradient are about to be changed.
+// parameter is given other memory, another size, type, layout or device.
 PyObject* gradients(PyObject* const* args, Py_ssize_t count) {
   if (count != 4 || !PyBytes_Check(args[3])) {
     PyErr_SetString(PyExc_TypeError, "gradients(gradients, parameters, device, types)");
@@ -174,10 +173,30 @@ PyObject* gradients(PyObject* const* args, Py_ssize_t count) {
     }
     data_of<uint64_t>(addresses)[i] = address;
   }
-  for (Py_ssize_t i = 0; i < n; ++i)
-    if (PySequence_Fast_GET_ITEM(grads.o, i) != Py_None)
-      changes(THPVariable_Unpack(PySequence_Fast_GET_ITEM(params.o, i)));
   return Py_BuildValue("OOO", addresses.o, types.o, places.o);
+}
+// stepped(gradients, parameters): the parameters with a gradient have been changed.
+PyObject* stepped(PyObject* const* args, Py_ssize_t count) {
+  if (count != 2) {
+    PyErr_SetString(PyExc_TypeError, "stepped(gradients, parameters)");
+    return nullptr;
+  }
+  Held grads(PySequence_Fast(args[0], "a list of gradients is wanted"));
+  Held params(PySequence_Fast(args[1], "a list of parameters is wanted"));
+  if (!grads || !params) return nullptr;
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(params.o);
+  if (PySequence_Fast_GET_SIZE(grads.o) != n) {
+    PyErr_Format(PyExc_ValueError, "%zd gradients wanted, got %zd", n,
+                 PySequence_Fast_GET_SIZE(grads.o));
+    return nullptr;
+  }
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (PySequence_Fast_GET_ITEM(grads.o, i) == Py_None) continue;
+    const at::Tensor* p = tensor_of(PySequence_Fast_GET_ITEM(params.o, i), "a parameter");
+    if (p == nullptr) return nullptr;
+    changes(*p);
+  }
+  Py_RETURN_NONE;
 }
 
 // ------------------------------------------------------------------------------ gradient norm
@@ -452,6 +471,7 @@ PyMethodDef method(const char* name, const char* doc) {
 PyMethodDef methods[] = {
     method<bind>("bind", "the library's entry points"),
     method<gradients>("gradients", "(addresses, types, parameters' places) of gradients"),
+    method<stepped>("stepped", "the parameters with a gradient have been changed"),
     method<grad_norm>("grad_norm", "(status, norm, factor) of a list of gradients, or None"),
     method<qk_forward>("qk_forward", "(status, q, k), or None"),
     method<qk_backward>("qk_backward", "(status, dq, dk, dgamma_q, dgamma_k), or None"),

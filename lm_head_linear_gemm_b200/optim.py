@@ -245,6 +245,7 @@ class AdamW:
                 int(self.skip_nonfinite), self._scratch.data_ptr(), handle)
         if rc != _abi.FLCE_OK:
             raise _abi.FlceError(rc, "flce_adamw_step")
+        _abi.marshal().stepped(grads, self.params)
 
     def status(self) -> int:
         """Device status bits of the steps so far (DEV_TIMEOUT: a wait inside a kernel ran out and

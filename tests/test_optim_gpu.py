@@ -448,6 +448,29 @@ def test_a_parameter_left_alone_stays_usable_in_its_graph(cuda_device):
     assert bool((p.grad == 4).all()) and not bool((q == 2).any())
 
 
+@pytest.mark.parametrize("why", ["eps", "factor", "gradient", "moved"])
+def test_a_refused_step_leaves_the_parameters_graphs_usable(cuda_device, why):
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    p, q = (torch.full((300,), 2.0, device="cuda", requires_grad=True) for _ in range(2))
+    opt = flce.AdamW([p, q], lr=0.1)
+    y, g = (p * p).sum(), [torch.ones(300, device="cuda") for _ in range(2)]
+    scale = None
+    if why == "eps":
+        opt.param_groups[0]["eps"] = 0.0
+    elif why == "factor":
+        scale = torch.ones(1, dtype=torch.float64, device="cuda")
+    elif why == "gradient":
+        g[1] = g[1].half()
+    else:
+        q.data = q.data[:100]
+        g[1] = g[1][:100]
+    with pytest.raises((flce.FlceError, TypeError, ValueError)):
+        opt.step(g, grad_scale=scale)
+    y.backward()
+    assert bool((p.grad == 4).all()) and int(opt.step_count) == 0
+
+
 def test_a_lone_tensor_is_one_parameter(cuda_device):
     import torch
     import lm_head_linear_gemm_b200 as flce
