@@ -368,9 +368,11 @@ struct Result {
     return gamma != Py_None && vector_of(o, *in.q, at::kFloat, in.shape.D, &unused);
   }
   void make() {
-    if (given == nullptr) return;
-    t = THPVariable_Unpack(given);
-    changes(t);
+    if (given != nullptr) t = THPVariable_Unpack(given);
+  }
+  // The call has been made, and has not refused.
+  void written() const {
+    if (given != nullptr) changes(t);
   }
   void make_rows(flce_qk_view* v) {
     make();
@@ -414,6 +416,7 @@ PyObject* qk_forward(PyObject* const* args, Py_ssize_t count) {
                            static_cast<const float*>(in.inv_freq), in.positions,
                            in.positions_batch, &qv, in.keys(kv), stream);
   });
+  if (rc == FLCE_OK) q.written(), k.written();
   return Py_BuildValue("iNN", rc, q.object(), k.object());
 }
 
@@ -449,6 +452,7 @@ PyObject* qk_backward(PyObject* const* args, Py_ssize_t count) {
                             in.positions, in.positions_batch, &qv, in.keys(kv), to_q, to_k,
                             accumulate, workspace, bytes, stream);
   });
+  if (rc == FLCE_OK) q.written(), k.written(), gamma_q.written(), gamma_k.written();
   return Py_BuildValue("iNNNN", rc, q.object(), k.object(), gamma_q.object(), gamma_k.object());
 }
 
