@@ -89,8 +89,8 @@ def build_marshal(force: bool = False, quiet: bool = False) -> str:
     return MARSHAL_PATH
 
 
-def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
-    build_marshal(force, quiet)
+def build_library(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
+    """``libflce.so``: needs nvcc alone."""
     if not force and not is_stale():
         return LIB_PATH
     tmp = LIB_PATH + ".tmp"
@@ -104,6 +104,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
         print(res.stderr, file=sys.stderr)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
+
+
+def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
+    """Both.  The library comes first: C callers use it without the binding's helper, which needs
+    torch's C++ headers."""
+    path = build_library(force, verbose_ptxas, quiet)
+    build_marshal(force, quiet)
+    return path
 
 
 if __name__ == "__main__":
