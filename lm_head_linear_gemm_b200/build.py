@@ -59,10 +59,24 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS)
 
 
+def marshal_built_for() -> str:
+    """What the helper is good for: it uses torch's C++ interface (internal parts of it too, tried
+    with torch 2.11), which no other version need share, and Python's."""
+    import torch
+    return f"built for torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def marshal_is_stale() -> bool:
+    if not os.path.exists(MARSHAL_PATH) or \
+            os.path.getmtime(MARSHAL_PATH) < max(map(os.path.getmtime, MARSHAL_SOURCES)):
+        return True
+    with open(MARSHAL_PATH, "rb") as f:                  # the module's attribute `built_for`
+        return marshal_built_for().encode() + b"\0" not in f.read()
+
+
 def build_marshal(force: bool = False, quiet: bool = False) -> str:
     """The host helper of the binding: a CPython module on torch's C++ headers (no kernels)."""
-    if not force and os.path.exists(MARSHAL_PATH) and \
-            os.path.getmtime(MARSHAL_PATH) >= max(map(os.path.getmtime, MARSHAL_SOURCES)):
+    if not force and not marshal_is_stale():
         return MARSHAL_PATH
     import sysconfig
 
@@ -73,6 +87,7 @@ def build_marshal(force: bool = False, quiet: bool = False) -> str:
         raise RuntimeError("g++ not found; it is required to build _marshal.so")
     tmp = MARSHAL_PATH + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
+           f'-DFLCE_MARSHAL_BUILT_FOR="{marshal_built_for()}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(base, "include"),
            "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),

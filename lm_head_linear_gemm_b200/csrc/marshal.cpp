@@ -486,4 +486,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch and the Python that it was built for: the build looks whether they are still there
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", FLCE_MARSHAL_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
