@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import argparse
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -82,11 +83,11 @@ def build_marshal(force: bool = False, quiet: bool = False) -> str:
 
     import torch
     base = os.path.dirname(torch.__file__)
-    cxx = shutil.which(os.environ.get("CXX", "g++"))
-    if cxx is None:
-        raise RuntimeError("g++ not found; it is required to build _marshal.so")
+    cxx = shlex.split(os.environ.get("CXX", "")) or ["g++"]  # may be several words ("ccache g++")
+    if shutil.which(cxx[0]) is None:
+        raise RuntimeError(f"{cxx[0]}: compiler not found; g++ (or CXX) builds _marshal.so")
     tmp = MARSHAL_PATH + ".tmp"
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [*cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
            f'-DFLCE_MARSHAL_BUILT_FOR="{marshal_built_for()}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(base, "include"),
@@ -99,7 +100,7 @@ def build_marshal(force: bool = False, quiet: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, MARSHAL_PATH)
     return MARSHAL_PATH
 
