@@ -28,8 +28,9 @@ extern "C" {
  *   pairs: interleaved = 0: a = i, b = i + rot/2;  interleaved = 1: a = 2i, b = 2i + 1.
  *   Elements rot .. D-1 are normed only.  rot = 0: no rotation.
  * Norm and rotation run in fp32 and the result is rounded once.  The angle is formed in 64 bits and
- * reduced by whole turns before the sine and cosine are taken in fp32: its error is about
- * |position * inv_freq| 2^-52, so positions may be far (or negative).
+ * reduced by whole turns before the sine and cosine are taken in fp32 (with what fp32 loses of the
+ * reduced angle made up for): its error is about |position * inv_freq| 2^-52, so positions may be
+ * far (or negative).
  */
 typedef struct {
   int64_t B, T;          /* sequences, tokens of each; B * T < 2^31; 0 allowed */

@@ -193,16 +193,20 @@ __device__ __forceinline__ void qk_store(T* chunk, int step, const QkPairs& p) {
 
 // cos and sin of every pair at this position, formed once by the warp.  The angle in turns is a
 // product in 64 bits (with the frequencies in turns, s_freq) less its nearest integer, so that far
-// positions lose nothing; what is left, |x| <= 1/2 turn, takes fp32.
+// positions lose nothing.  Of what is left, |x| <= 1/2 turn, the sine and cosine are taken in fp32;
+// what fp32 loses of x (up to 2^-26 turns, 9e-8 rad, more than a sine's own rounding) turns them on:
+// its square is below 2^-46.
 __device__ __forceinline__ void qk_angles(int lane, double pos, const double* s_freq, int half,
                                           float2* s_cs) {
   __syncwarp();                        // the previous token's values are read
   for (int i = lane; i < half; i += 32) {
     const double turns = pos * s_freq[i];
-    const float part = static_cast<float>(turns - rint(turns));
-    float2 cs;
-    sincospif(2.f * part, &cs.y, &cs.x);
-    s_cs[i] = cs;
+    const double rest = turns - rint(turns);
+    const float part = static_cast<float>(rest);
+    const float low = static_cast<float>(rest - static_cast<double>(part)) * 6.283185307f;
+    float c, s;
+    sincospif(2.f * part, &s, &c);
+    s_cs[i] = make_float2(fmaf(-s, low, c), fmaf(c, low, s));
   }
   __syncwarp();
 }
