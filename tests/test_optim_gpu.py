@@ -225,6 +225,30 @@ def test_many_tensors_groups_and_missing_gradients(cuda_device):
     assert int(opt.step_count) == 2
 
 
+@pytest.mark.parametrize("count", [40, 450])
+def test_long_launches_of_every_type_at_once(cuda_device, count):
+    """More elements than the short tiling takes, in tensors of every type, width and alignment with
+    whole tiles and tails: a launch's ring has stages for the widest of them.  450 tensors, all with
+    a gradient, take two launches."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    rng = np.random.default_rng(count)
+    sizes = rng.integers(1, 2 * 6_000_000 // count, count)
+    assert sizes.sum() > 5_000_000
+    made = [_make(int(n), *KINDS[i % len(KINDS)], seed=i, offset=(0, 0, 0, 1)[i % 4])
+            for i, n in enumerate(sizes)]
+    before = [_before(*x) for x in made]
+    other = dict(lr=0.003, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0)
+    cut = count // 3
+    opt = flce.AdamW([dict(params=[x[0] for x in part], states=[x[2] for x in part], **h)
+                      for part, h in ((made[:cut], GROUP), (made[cut:], other))],
+                     step=torch.full((1,), 9, dtype=torch.int64, device="cuda"))
+    opt.step([x[1] for x in made], grad_scale=0.5)
+    assert int(opt.step_count) == 10 and not opt._scratch.any()
+    for i, (b, (p, _, s)) in enumerate(zip(before, made)):
+        _check(b, p, s, 10, scale=0.5, **(GROUP if i < cut else other))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_run_from_zero_states_against_the_oracle(cuda_device, bits):
     """Six steps from fresh states; each is checked from what the one before it left."""
@@ -678,6 +702,24 @@ def test_grad_norm(cuda_device, dtype, offset):
                      ([grads[5], grads[5].double()], TypeError), ([grads[6][::2]], ValueError)):
         with pytest.raises(err):
             flce.grad_norm(bad)
+
+
+def test_grad_norm_of_many_large_tensors(cuda_device):
+    """More tensors than the small launch takes, with whole chunks, tails, both types, any alignment."""
+    import torch
+    import lm_head_linear_gemm_b200 as flce
+    rng = np.random.default_rng(12)
+    grads = []
+    for i in range(1100):                                 # two launches
+        n, offset = int(rng.integers(1, 60000 if i % 10 == 0 else 2000)), i % 3
+        t = torch.zeros(n + offset, dtype=_dtype(("bf16", "f32")[i % 2]), device="cuda")[offset:]
+        t.copy_(torch.from_numpy(rng.standard_normal(n) * 10.0 ** rng.uniform(-4, 0)))
+        grads.append(t)
+    assert sum(g.numel() >= 16384 for g in grads) > 50
+    want, wf = ot.grad_norm([_np(g) for g in grads], 0.5)
+    norm, factor = flce.grad_norm(grads, 0.5)
+    assert abs(float(norm) - want) <= 34 * U * want and abs(float(factor) - wf) <= 40 * U * wf
+    assert torch.equal(norm, flce.grad_norm(grads)[0])
 
 
 def test_grad_norm_of_many_none_zero_and_nan(cuda_device):
