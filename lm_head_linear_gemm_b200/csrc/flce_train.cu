@@ -281,7 +281,10 @@ AdamGroup adamw_group(const flce_adamw_group& g) {
   return o;
 }
 
-// A stage of the ring holds a tile of the launch's widest tensor; the ring as many stages as fit.
+// A stage of the ring holds a tile of the launch's widest tensor; the ring as many stages as fit.  All
+// tensors count, those too short or too unaligned to enter the ring among them: a norm's weights with
+// fp32 states next to matrices in 8 bits leave one stage of two (77 M weights 132 -> 182 us, 236 M
+// with master copies 635 -> 654).
 template <typename Args>
 void adamw_stage(Args* a) {
   constexpr int kTile = Args::kTile;

@@ -4,10 +4,11 @@
 // tensors' descriptors travel in the launch's parameters, so a step needs no table on the device
 // and may be captured with the pointers it was given.
 //
-// One B200 (a copy runs at 6.57 TB/s).  AdamW on 77 M bf16 weights: fp32 states and gradient 293 us,
-// 6.3 TB/s; 8-bit states, bf16 gradient 135 us, 5.8 TB/s, where the instructions (58% of the issue
-// slots: conversions, roundings) and the memory bound it together; 236 M weights with master copies
-// 632 us, 6.0 TB/s.  Norm of 236 M bf16 values 70 us, 6.7 TB/s.
+// One B200 (a copy runs at 6.57 TB/s), a call: AdamW on 77 M bf16 weights, fp32 states and gradient
+// 292 us, 6.3 TB/s; 8-bit states throughout, bf16 gradient 132 to 144 us with the clock, 5.4 to
+// 5.9 TB/s, where the instructions (56% of the issue slots: conversions, roundings) and the memory
+// bound it together; 236 M weights with master copies 629 to 638 us, 6.0 TB/s.  Norm of 236 M bf16
+// values 74 to 76 us, 6.2 to 6.4 TB/s.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -323,7 +324,9 @@ struct AdamTile {
 constexpr int kTileParam16 = 1, kTileGrad16 = 2, kTileMaster = 4, kTileState8 = 8;
 
 // A part of a tile that its tensor ends in, or with any alignment, straight from global memory.  Each warp
-// takes 256 consecutive elements: one block of an 8-bit state.
+// takes 256 consecutive elements: one block of an 8-bit state.  Unaligned it loads and stores element by
+// element: 77 M weights and gradients one element off take 568 us with fp32 states (292 aligned), 470
+// with 8-bit states (132).
 __device__ __forceinline__ void adamw_ragged(const AdamTile& T, const AdamScalars& a, int part) {
   const int tid = threadIdx.x, at = part * kAdamPart + 8 * tid, warp = at / kStateBlock;
   if (at - 8 * (tid & 31) >= T.n) return;              // a warp's 256 elements, or none
@@ -396,8 +399,10 @@ __device__ __forceinline__ int find_tensor(const uint32_t* first, int count, uin
 
 // ------------------------------------------------------------------ the walk over the tiles
 // A warp of its own walks over the block's tiles, hands each to the other warps, and brings the
-// whole ones into shared memory, several tiles ahead: the elements by bulk copies, the scales, which
-// may lie at any multiple of 4 bytes, by a copy of each.  What is in flight does not depend on the
+// whole ones into shared memory, ahead of their use by as many tiles as the ring has stages (long
+// tiles: two with 8-bit states, one where a tensor of the launch has fp32 states): the elements by
+// bulk copies, the scales, which may lie at any multiple of 4 bytes, by a copy of each.  What is in
+// flight does not depend on the
 // registers of the warps that compute, and neither the copies nor the descriptors cost them
 // instructions.
 __device__ __forceinline__ void scale_load(uint32_t dst, const void* src) {
@@ -739,7 +744,8 @@ __device__ __forceinline__ float norm_chunk(const void* grad, long long start) {
   }
   return acc;
 }
-// The same of a chunk that the tensor ends in, or with any alignment.
+// The same of a chunk that the tensor ends in, or with any alignment (element by element: 236 M bf16
+// values one element off take 160 us, 75 aligned).
 __device__ __forceinline__ float norm_ragged(const NormTensor& T, long long start) {
   float acc = 0.f;
 #pragma unroll 1

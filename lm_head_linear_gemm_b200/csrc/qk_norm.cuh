@@ -8,9 +8,11 @@
 // takes no registers; the arithmetic is in pairs of fp32 (two operations in an instruction): one at
 // a time it took longer than the memory.
 //
-// 16 x 1024 tokens of 32 + 8 heads of 128 in bf16, one B200 (a copy runs at 6.57 TB/s): forward 57 us,
-// 5.9 TB/s; backward 89 us, 5.6 TB/s, with half of the issue slots taken.  One token: 3.9 us, the
-// latency of a launch, a row and a store.
+// 16 x 1024 tokens of 32 + 8 heads of 128 in bf16, one B200 (a copy runs at 6.57 TB/s), a call: forward
+// 59 us, 5.7 TB/s; backward 90 to 96 us, 5.2 to 5.6 TB/s, with half of the issue slots taken.  In fp32
+// 116 us, 5.8 TB/s, and 172, 5.9.  One token: 3.8 us of GPU time, the latency of a launch, a row and a
+// store.  The backward is held to 128 registers (two blocks on an SM) and all but two of its 40
+// instances spill a little: 8 to 28 bytes a thread, 40 to 76 with 3, 5, 6 or 10 lanes to a row.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -260,7 +262,8 @@ struct QkRing {
   static constexpr int kRow = 16 * sizeof(T);              // bytes of a lane's 16 elements
   static constexpr int kSlot = 32 * kRow * (BWD ? 2 : 1);  // x, and dy
   // Three passes: more in flight ran slower (forward of 16k tokens 59 us with 3, 62 with 2, 64 with
-  // 4, 65 with 8 slots).  fp32 backward: two, so that two blocks fit an SM.
+  // 4, 65 with 8 slots).  fp32 backward: two, so that two blocks fit an SM up to heads of 256 (above,
+  // with 22 KB for angles and gammas, one does).
   static constexpr int kSlots = BWD && sizeof(T) == 4 ? 2 : 3;
   static constexpr int kWarp = kSlots * kSlot;
   // the backward's sums of d xh: 16 elements of each lane for q and for k

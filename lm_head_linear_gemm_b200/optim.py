@@ -63,10 +63,14 @@ class AdamW:
     or bfloat16 CUDA tensors on one device; gradients may be float32 or bfloat16 whatever the
     parameter's type.  The groups stand in ``param_groups`` and their numbers may be changed between
     steps; ``lr`` may be a one-element float32 device tensor, which a captured step reads anew.
+    It is no ``torch.optim.Optimizer``: it has no ``zero_grad`` (set the gradients to None), and torch's
+    learning-rate schedulers do not take it (write the rate into the group, or into its tensor).
 
     ``state_bits`` = 32: ``m`` and ``v`` in float32.  8: e4m3 codes of m and of r = sqrt(v) with a
     float32 scale for every 256 elements, for tensors of at least ``min_8bit_size`` elements (a
-    small tensor's states stay in 32 bits).  ``master_weights``: bf16 parameters get a float32 copy
+    small tensor's states stay in 32 bits; 0 puts all in 8 bits, which is faster: a launch with one
+    tensor of fp32 states keeps fewer tiles in flight).  A tensor with an array off its alignment
+    (fp32 at 32 bytes, others at 16) is stepped element by element, two to four times slower.  ``master_weights``: bf16 parameters get a float32 copy
     that takes the update; the parameter is its rounding.  ``states`` of a group adopts the caller's
     tensors instead of zeros: for each parameter a dict with ``m`` and ``v``, or ``m``, ``r``,
     ``m_scale`` and ``r_scale``, and ``master`` where there is one.
@@ -75,7 +79,8 @@ class AdamW:
     tensors not replaced.  ``step_count`` [1] int64 on the device counts the steps done (``step=``
     adopts the caller's).  Every parameter shares it: one without a gradient in a step is left as it
     is.  With ``skip_nonfinite`` a step whose ``grad_scale`` is not finite (grad_norm's factor after an
-    overflow) changes nothing and is not counted."""
+    overflow) changes nothing and is not counted.  An optimizer's steps follow one another: they must
+    not overlap on the GPU (on two streams, or in two graphs replayed at once)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, min_8bit_size: int = 4096,

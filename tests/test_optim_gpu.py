@@ -399,7 +399,7 @@ def test_a_number_as_the_factor_waits_for_nothing(cuda_device, scale):
         opts[1].step([g], grad_scale=scale)
     graph.replay()
     torch.cuda.synchronize()
-    torch.cuda._sleep(200_000_000)                        # about 0.1 s
+    torch.cuda._sleep(1_000_000_000)                      # about 0.5 s
     opts[2].step([g], grad_scale=scale)
     assert not torch.cuda.current_stream().query()
     assert torch.equal(made[0], made[1]) and torch.equal(made[0], made[2])
