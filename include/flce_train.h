@@ -131,8 +131,9 @@ typedef struct {
 /*
  *   tensors, grads [count]: host arrays, read before the call returns.  grads[i] is a device
  *     pointer to n elements of grad_dtype; NULL leaves tensor i as it is.
- *   No two tensors may overlap.  Pointers need their element's alignment only; the fast path
- *     takes fp32 arrays at 32 and bf16 arrays and codes at 16 bytes.
+ *   No two tensors may overlap, nor a gradient another tensor's arrays (a step writes its tensors in
+ *     any order).  Pointers need their element's alignment only; the fast path takes fp32 arrays at
+ *     32 and bf16 arrays and codes at 16 bytes.
  *   groups [n_groups], 1 <= n_groups <= FLCE_ADAMW_MAX_GROUPS: host array.
  *   step: device int64, the steps done so far; the call adds 1.  8-byte aligned.
  *   skip_nonfinite = 1: a grad_scale that is not finite (flce_grad_norm of gradients with an

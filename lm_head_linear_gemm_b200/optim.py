@@ -70,10 +70,11 @@ class AdamW:
     float32 scale for every 256 elements, for tensors of at least ``min_8bit_size`` elements (a
     small tensor's states stay in 32 bits; 0 puts all in 8 bits, which is faster: a launch with one
     tensor of fp32 states keeps fewer tiles in flight).  A tensor with an array off its alignment
-    (fp32 at 32 bytes, others at 16) is stepped element by element, two to four times slower.  ``master_weights``: bf16 parameters get a float32 copy
-    that takes the update; the parameter is its rounding.  ``states`` of a group adopts the caller's
-    tensors instead of zeros: for each parameter a dict with ``m`` and ``v``, or ``m``, ``r``,
-    ``m_scale`` and ``r_scale``, and ``master`` where there is one.
+    (fp32 at 32 bytes, others at 16) is stepped element by element, two to four times slower.
+    ``master_weights``: bf16 parameters get a float32 copy that takes the update; the parameter is
+    its rounding. ``states`` of a group adopts the caller's tensors instead of zeros: for each
+    parameter a dict with ``m`` and ``v``, or ``m``, ``r``, ``m_scale`` and ``r_scale``, and
+    ``master`` where there is one.
 
     ``state`` has a read-only dict of tensors for each parameter: their values may be written, the
     tensors not replaced.  ``step_count`` [1] int64 on the device counts the steps done (``step=``
